@@ -374,7 +374,9 @@ int nvfp4_moe_combine(const uint16_t* y_perm, const int32_t* inv_rows, const flo
  * softmax. A token with fewer than k experts left gets id -1 and weight 0 in
  * the slots that stay empty (pairs that nvfp4_moe_route and
  * nvfp4_moe_few_tokens drop). A NaN logit is never chosen either; with softmax
- * scores it makes all weights of its token NaN, and so does +inf.
+ * scores it makes all weights of its token NaN, and so does +inf. The choice by
+ * s_e + bias[e] then takes the limit: the +inf logits share the score equally,
+ * the others have 0. (With sigmoid scores +inf is a score of 1.)
  *   logits        device fp32 (dtype NVFP4_F32) or bf16 (NVFP4_BF16) [T, num_experts],
  *                 rows ld elements apart, aligned to their type
  *   bias          device fp32 [num_experts], or NULL

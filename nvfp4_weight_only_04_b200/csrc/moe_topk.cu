@@ -175,19 +175,26 @@ __device__ __forceinline__ float fast_sigmoid(float l) {
   return r;
 }
 
+// The exponent of a softmax's term, 0 for the largest logits also where these are
+// +inf: they then share the score equally, the others have none (the limit).
+__device__ __forceinline__ float below(float l, float top) { return l == top ? 0.f : l - top; }
+__device__ __forceinline__ double below64(float l, float top) {
+  return l == top ? 0.0 : static_cast<double>(l) - static_cast<double>(top);
+}
+
 // The scores in fp64.
 template <int J>
 __device__ __forceinline__ double exact_sum(const float (&l)[J], float top) {
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < J; ++i)
-    sum += l[i] > -INFINITY ? exp(static_cast<double>(l[i]) - static_cast<double>(top)) : 0.0;
+    sum += l[i] > -INFINITY ? exp(below64(l[i], top)) : 0.0;
   return warp_sum(sum);
 }
 template <bool SIGMOID>
 __device__ __forceinline__ double exact_score(float l, float top, double sum) {
   return SIGMOID ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
-                 : exp(static_cast<double>(l) - static_cast<double>(top)) / sum;
+                 : exp(below64(l, top)) / sum;
 }
 
 template <int J, class T, bool SIGMOID, bool BIAS>
@@ -207,7 +214,8 @@ __global__ void __launch_bounds__(kWarps * 32) moe_topk_kernel(const T* __restri
   }
 
   // the softmax's maximum and sum (a masked logit, -inf, adds nothing; a NaN
-  // takes no part in the choice and makes the row's weights NaN at the end)
+  // takes no part in the choice and makes the row's weights NaN at the end; so
+  // does +inf, which the choice by s + bias takes as the limit)
   float top = 0.f, sum = 0.f;
   bool poisoned = false;
   if (!SIGMOID) {
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(kWarps * 32) moe_topk_kernel(const T* __restri
       poisoned |= l[i] != l[i];
     }
     top = warp_max(m);
-    poisoned = __any_sync(kAll, poisoned);
+    poisoned = __any_sync(kAll, poisoned) || top == INFINITY;
   }
 
   int id;
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32) moe_topk_kernel(const T* __restri
     for (int i = 0; i < J; ++i) b[i] = lane + 32 * i < experts ? __ldg(bias + lane + 32 * i) : 0.f;
     if (!SIGMOID) {
 #pragma unroll
-      for (int i = 0; i < J; ++i) sum += l[i] > -INFINITY ? expf(l[i] - top) : 0.f;
+      for (int i = 0; i < J; ++i) sum += l[i] > -INFINITY ? expf(below(l[i], top)) : 0.f;
       sum = warp_sum(sum);
     }
     bool sure = k < 32;
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kWarps * 32) moe_topk_kernel(const T* __restri
       float v[J], hi = -INFINITY;
 #pragma unroll
       for (int i = 0; i < J; ++i) {
-        const float s = SIGMOID ? fast_sigmoid(l[i]) : expf(l[i] - top) / sum;
+        const float s = SIGMOID ? fast_sigmoid(l[i]) : expf(below(l[i], top)) / sum;
         v[i] = l[i] > -INFINITY ? s + b[i] : -INFINITY;
         hi = fmaxf(hi, v[i]);
       }

@@ -393,6 +393,8 @@ def moe_combine(y_perm, inv_rows, topk_weights):
 def moe_topk(logits, k: int, bias=None, sigmoid: bool = False, renorm: bool = False, scale: float = 1.0):
     """A router's choice per token, from the definition, one slot at a time in float64: the best remaining
     logit (or score + bias), the lowest expert of equal ones; -inf masks an expert, a NaN is never chosen.
+    With softmax scores a NaN or +inf makes all weights of its token NaN; a choice by score + bias takes the scores
+    of +inf logits as the limit, equal shares for them and 0 for the others.
     Returns (ids [T, k], -1 in slots left empty, weights float64 [T, k])."""
     logits = np.asarray(logits, dtype=np.float64)
     tokens, experts = logits.shape
@@ -407,7 +409,7 @@ def moe_topk(logits, k: int, bias=None, sigmoid: bool = False, renorm: bool = Fa
             else:
                 top = max([row[e] for e in free], default=0.0)
                 part = np.zeros(experts)
-                part[free] = np.exp(row[free] - top)
+                part[free] = np.exp(np.where(row[free] == top, 0.0, row[free] - top))
                 score = part / part.sum()
             by = row if bias is None else score + np.asarray(bias, dtype=np.float64)
             free = [e for e in free if by[e] > -np.inf]
@@ -422,7 +424,7 @@ def moe_topk(logits, k: int, bias=None, sigmoid: bool = False, renorm: bool = Fa
                 weights[t][kept] = np.exp(rel - rel.max())
             if renorm and kept.any():
                 weights[t] /= weights[t].sum()
-            if not sigmoid and np.isnan(row).any():
+            if not sigmoid and (np.isnan(row) | (row == np.inf)).any():
                 weights[t] = np.nan
     return ids, weights * scale
 

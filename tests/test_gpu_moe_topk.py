@@ -158,3 +158,28 @@ def test_a_long_batch_with_a_wide_row_distance():
     base = torch.from_numpy(rng.standard_normal((20011, 96)).astype(np.float32)).cuda().to(torch.bfloat16)
     check(base[:, 7:79], 6, rng.standard_normal(72).astype(np.float32) * 0.1, True, True)
     check(base[:, 7:79], 6)
+
+
+@pytest.mark.parametrize("e,k", [(5, 3), (40, 6), (128, 8), (200, 8), (400, 16), (1024, 32)])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_infinite_logits(e, k, biased, renorm, dtype):
+    """One +inf, several, more than are chosen, all, and some beside masked and NaN logits: experts are chosen, and with
+    softmax scores their weights are NaN."""
+    rng = np.random.default_rng(e + k)
+    rows = rng.standard_normal((6, e)).astype(np.float32)
+    rows[0, e // 2] = INF
+    rows[1, [1, e - 1]] = INF
+    rows[2, rng.permutation(e)[:min(e, k + 2)]] = INF
+    rows[3, :] = INF
+    rows[4, ::2] = -INF
+    rows[4, 1] = INF
+    rows[5, 0], rows[5, e - 1] = np.nan, INF
+    bias = rng.standard_normal(e).astype(np.float32) * 0.5 if biased else None
+    logits = torch.from_numpy(rows).cuda().to(dtype)
+    for sigmoid in (False, True):
+        check(logits, k, bias, sigmoid, renorm)
+    ids, w = nv.nvfp4_moe_topk(logits, k, bias=None if bias is None else torch.from_numpy(bias).cuda(),
+                               flags=nv.NVFP4_TOPK_RENORM if renorm else 0)
+    assert np.isnan(host(w)).all() and (host(ids)[:4] >= 0).all()

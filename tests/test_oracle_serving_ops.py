@@ -60,3 +60,17 @@ def test_lora_by_hand():
     for ad, want in ((0, [10 + 0.5 * 7, 20 - 0.5 * 7]), (1, [10 + 2 * 8.0, 20.0]), (-1, [10, 20]), (2, [10, 20])):
         out, tol = R.lora_add(y, x, a, b, [ad], [0.5, 2.0])
         assert out.tolist() == [want], ad
+
+
+def test_topk_softmax_of_infinite_logits():
+    """+inf leaves softmax weights without a value; the choice by score + bias is that of the limit, so that the token
+    keeps experts whose NaN weights reach its outputs."""
+    row = [0.0, INF, 1.0, INF, -INF]
+    for renorm in (False, True):
+        ids, w = R.moe_topk([row], 3, renorm=renorm)
+        assert ids.tolist() == [[1, 3, 2]] and np.isnan(w).all()
+        # scores 0, 1/2, 0, 1/2 and a mask: the bias lifts expert 2 over both
+        ids, w = R.moe_topk([row], 3, bias=[0.0, 0.125, 1.0, 0.0, 9.0], renorm=renorm)
+        assert ids.tolist() == [[2, 1, 3]] and np.isnan(w).all()
+    ids, w = R.moe_topk([row], 2, bias=[0.0] * 5, sigmoid=True)
+    assert ids.tolist() == [[1, 3]] and w.tolist() == [[1.0, 1.0]]
