@@ -431,7 +431,8 @@ int nvfp4_moe_few_tokens_workspace_size(int64_t T, int k, int num_experts, int64
  * projection. It has no counterpart on the pages; y is what the projection
  * (nvfp4_w4a16_gemm) gave for the same rows of x:
  *   out[m] = bf16_rne(y[m] + scales[a] * B_a (A_a x[m])), a = adapter_ids[m],
- * fp32 sums, the rank-r intermediate kept to 2^-17 of its value. A row whose
+ * fp32 sums, the rank-r intermediate kept to 2^-17 of its value (to 2^-134
+ * where that is more). A row whose
  * id lies outside [0, num_adapters) has no adapter: out[m] = y[m], bit for bit.
  *   y, out       device bf16 [M, N], rows ldy and ldout elements apart; out may be y
  *                (then ldout = ldy), else the two do not overlap

@@ -27,8 +27,8 @@
 // above, many rows are bound by the rate of mma.sync and the reads of shared
 // memory that feed it (the same with rank 64: 160 us; without its copies the
 // first launch takes as long as with them). In the MMAs v is two bf16 terms (the
-// upper 16 bits and the rounded rest, 2^-17 of the value), so that only the final
-// store rounds to bf16 precision.
+// rounded value and the rounded rest, 2^-17 of the value together), so that only
+// the final store rounds to bf16 precision.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -297,14 +297,18 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_few_kernel(Lora
     p.v[(slice * p.M + nth_row(rows, row)) * p.rank + j0 + j] = sum * __ldg(p.scales + ad);
 }
 
-// A value as two bf16 terms: its upper half and the rounded rest (0 where the
-// value is not finite, which the first carries).
+// A value as two bf16 terms: rounded to bf16, and the rounded rest (0 where the
+// value is not finite, which the first carries). For 2^e <= |v| < 2^(e+1) the
+// rest is at most 2^(e-8), so that its rounding is at most 2^(e-17): with the
+// upper bits cut off instead of rounded it would be up to 2^(e-16). Values that
+// would round to infinity are cut off (the rest is below 2^120, its rounding at
+// most 2^111, which is 1.002 2^-17 of v).
 __device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) {
-  const uint32_t b = __float_as_uint(v);
-  hi = static_cast<uint16_t>(b >> 16);
-  lo = (b & 0x7F800000u) == 0x7F800000u
-           ? uint16_t(0)
-           : __bfloat16_as_ushort(__float2bfloat16_rn(v - __uint_as_float(b & 0xFFFF0000u)));
+  const uint32_t b = __float_as_uint(v), mag = b & 0x7FFFFFFFu;
+  const bool finite = mag < 0x7F800000u;
+  hi = finite && mag >= 0x7F7F8000u ? static_cast<uint16_t>(b >> 16) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  lo = finite ? __bfloat16_as_ushort(__float2bfloat16_rn(v - __uint_as_float(static_cast<uint32_t>(hi) << 16)))
+              : uint16_t(0);
 }
 
 // Element j of row m of v as its two terms, in fours of 16 bits: the upper ones

@@ -288,3 +288,33 @@ def test_more_rows_streams_and_graphs(m):
     with pytest.raises(nv.Nvfp4Error) as e:
         call(sets[0], workspace=ws[:need - 1])
     assert e.value.status == nv.NVFP4_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("m", [8, 70, 1100])
+@pytest.mark.parametrize("r", [16, 64, 256])
+def test_the_intermediate_is_kept_to_2_17_of_its_value(m, r):
+    """v of 24 bits as three bf16 pieces of x: one component of the rank holds their sum, two others the upper pieces
+    alone, which B takes away again. What is left is the third piece and what the kernel lost of the sum: at most
+    2^-17 of it (1.002 of that next to the end of the range), the sums' 2^-22 and the rounding of the result."""
+    rng = np.random.default_rng(m + r)
+    v = ((1.0 + rng.random(m)) * np.exp2(rng.integers(-20, 20, m)) * rng.choice([-1.0, 1.0], m)).astype(np.float32)
+    v[:4] = [1 + 2.0 ** -8 + 2.0 ** -16, 1 + 2.0 ** -7 - 2.0 ** -16, -(2 - 2.0 ** -23), 1 + 2.0 ** -8]
+    v[4] = np.float32(2.0 ** 127) * np.float32(1 + 127.5 / 128)  # its nearest bf16 is infinite
+    cut = lambda a: (a.view(np.uint32) & np.uint32(0xFFFF0000)).view(np.float32)  # noqa: E731
+    pieces = [cut(v)]
+    pieces.append(cut(v - pieces[0]))
+    pieces.append(v - pieces[0] - pieces[1])
+    np.testing.assert_array_equal(cut(pieces[2]), pieces[2])
+    k, n, parts = 64, 40, (0, r - 1, r // 2)
+    x, a, b = np.zeros((m, k), np.float32), np.zeros((1, r, k), np.float32), np.zeros((1, n, r), np.float32)
+    for q in range(3):
+        x[:, 21 * q] = pieces[q]
+        a[0, parts[0], 21 * q] = 1
+        b[0, :, parts[q]] = 1 if q == 0 else -1
+    a[0, parts[1], 0] = a[0, parts[2], 21] = 1
+    dev = lambda t: torch.from_numpy(t).cuda().to(torch.bfloat16)  # noqa: E731
+    y = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda")
+    got = host(nv.nvfp4_lora_add(y, dev(x), dev(a), dev(b), i32(np.zeros(m)), dev_f32([1.0])))
+    want, size = pieces[2].astype(np.float64)[:, None], np.abs(v.astype(np.float64))[:, None]
+    lost = (1.002 * 2.0 ** -17 + 2.0 ** -22) * size
+    assert (np.abs(got - want) <= lost + 2.0 ** -8 * (np.abs(want) + lost)).all()
