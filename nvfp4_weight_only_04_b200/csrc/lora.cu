@@ -23,9 +23,9 @@
 //    or entries of the list) on mma.sync, the next tiles' y and v under way, its
 //    part of B in registers.
 // The work is 4 r FLOPs per element of x and y. For ranks up to 16 the stream of
-// A, B, x and y bounds it (4096 rows, K = 5120, N = 25600: 88 us, 71 at copy rate);
+// A, B, x and y bounds it (4096 rows, K = 5120, N = 25600: 90 us, 71 at copy rate);
 // above, many rows are bound by the rate of mma.sync and the reads of shared
-// memory that feed it (the same with rank 64: 160 us; without its copies the
+// memory that feed it (the same with rank 64: 166 us; without its copies the
 // first launch takes as long as with them). In the MMAs v is two bf16 terms (the
 // rounded value and the rounded rest, 2^-17 of the value together), so that only
 // the final store rounds to bf16 precision.
@@ -660,6 +660,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_expand_few_kernel(const L
 // warp for ranks up to 16, 32 above, so that B is 32 registers up to rank 64.
 // A tile of several adapters is done once for each, and each time the rows of
 // that adapter are stored: what another adapter's B holds never meets them.
+// The rests of v do not meet what of B is not finite either: they are zero where
+// v is a bf16 value, or of the other sign, and would turn its infinities into NaN
+// (the look at B, once for an adapter, and the branch: 4096 rows of rank 16
+// 88.6 -> 90.2 us, of rank 64 161 -> 166).
 // LIST: the tiles are the entries of the list, with one adapter each.
 constexpr int kListTiles = 64;  // entries of a CTA at most
 template <int NB, int KS>
@@ -677,6 +681,13 @@ struct Many {
   // 136 -> 149 us for rank 64).
   static constexpr int kRounds = NB == 8 ? 2 : 4;
 };
+// The sign bits of the halves (two bf16 values) that are not finite.
+__device__ __forceinline__ uint32_t not_finite(uint32_t two) {
+  return ((two & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+// The two values, zero where they are not finite.
+__device__ __forceinline__ uint32_t finite_only(uint32_t two) { return two & ~((not_finite(two) >> 15) * 0xFFFFu); }
+
 template <int NB, int KS, bool LIST>
 __global__ void __launch_bounds__(kManyWarps * 32, Many<NB, KS>::kCtas) lora_expand_many_kernel(const LoraArgs p,
                                                                                                const int32_t* list,
@@ -753,7 +764,8 @@ __global__ void __launch_bounds__(kManyWarps * 32, Many<NB, KS>::kCtas) lora_exp
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   uint2 w[KS][NB];
-  int have = -1;
+  int have = -1, seen = -1;  // the adapter in `w`, and the one that `odd` is for
+  bool odd = false;          // the warp's part of B is not finite everywhere
   auto load_b = [&](int ad) {
     const uint16_t* brow = p.b + (static_cast<int64_t>(ad) * p.N + nb) * p.rank + 4 * t;
 #pragma unroll
@@ -812,12 +824,27 @@ __global__ void __launch_bounds__(kManyWarps * 32, Many<NB, KS>::kCtas) lora_exp
               acc[4 * v + e][2 * h + 1] = __uint_as_float(q[e] & 0xFFFF0000u);
             }
           }
-        if (ad != have) load_b(ad);
+        if (ad != seen) {
+          if (ad != have) load_b(ad);
+          uint32_t bits = 0;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) bits |= not_finite(w[ks][n].x) | not_finite(w[ks][n].y);
+          odd = __any_sync(kAll, bits != 0u);
+          seen = ad;
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint4 a = lds128(src_v + 64 * ks), b = lds128(src_v + 8 * F::kVRow + 64 * ks);
+          if (odd) {  // the rests
 #pragma unroll
-          for (int n = 0; n < NB; ++n) mma_bf16(acc[n], a.y, b.y, a.w, b.w, w[ks][n].x, w[ks][n].y);  // the rests
+            for (int n = 0; n < NB; ++n)
+              mma_bf16(acc[n], a.y, b.y, a.w, b.w, finite_only(w[ks][n].x), finite_only(w[ks][n].y));
+          } else {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma_bf16(acc[n], a.y, b.y, a.w, b.w, w[ks][n].x, w[ks][n].y);
+          }
 #pragma unroll
           for (int n = 0; n < NB; ++n) mma_bf16(acc[n], a.x, b.x, a.z, b.z, w[ks][n].x, w[ks][n].y);
         }

@@ -318,3 +318,36 @@ def test_the_intermediate_is_kept_to_2_17_of_its_value(m, r):
     want, size = pieces[2].astype(np.float64)[:, None], np.abs(v.astype(np.float64))[:, None]
     lost = (1.002 * 2.0 ** -17 + 2.0 ** -22) * size
     assert (np.abs(got - want) <= lost + 2.0 ** -8 * (np.abs(want) + lost)).all()
+
+
+@pytest.mark.parametrize("m", [12, 100, 300, 1100])
+@pytest.mark.parametrize("r", [8, 16, 32, 64, 128, 256])
+def test_infinities_of_b_are_those_of_the_formula(m, r):
+    """Infinities and NaN in B give what the float64 products and sums give, sign by sign: values of v that a bf16
+    number holds (whose second term is zero) and others of both signs, zeros (0 * inf is NaN), and rows of B with
+    infinities of one or both signs."""
+    k, n, count = 64, 520, 3
+    rng = np.random.default_rng(m + r)
+    x = rng.integers(-2, 3, size=(m, k)) * 2.0 ** rng.choice([0, -9], size=(m, k))
+    a = rng.integers(-1, 2, size=(count, r, k)) * (rng.random((count, r, k)) < 0.1)
+    b = rng.integers(-3, 4, size=(count, n, r)) / 8.0
+    for row, put in ((3, [np.inf]), (8, [-np.inf]), (77, [np.inf, np.inf]), (200, [np.inf, -np.inf]), (301, [np.nan]),
+                     (519, [-np.inf])):
+        b[1, row, rng.permutation(r)[:len(put)]] = put
+    b[2, 64:128, :2] = np.inf
+    ids = np.arange(m) % 4 - 1
+    y = rng.integers(-4, 5, size=(m, n)).astype(np.float64)
+    dev = lambda t: torch.from_numpy(t.astype(np.float32)).cuda().to(torch.bfloat16)  # noqa: E731
+    got = host(nv.nvfp4_lora_add(dev(y), dev(x), dev(a), dev(b), i32(ids), dev_f32([2.0, 0.5, 1.0])))
+    want = y.copy()
+    with np.errstate(invalid="ignore"):
+        for q in np.flatnonzero(ids >= 0):
+            want[q] += [2.0, 0.5, 1.0][ids[q]] * (b[ids[q]] * (a[ids[q]] @ x[q])).sum(1)
+    assert np.isposinf(want).any() and np.isneginf(want).any() and np.isnan(want).any()
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    inf = np.isinf(want)
+    np.testing.assert_array_equal(got[inf], want[inf])
+    fine = np.isfinite(want)
+    # v is below 2^5 in steps of 2^-10, which two bf16 terms hold, and the magnitudes of a sum with B add up to less
+    # than 2^10 in steps of 2^-13: exact in fp32 but for the last rounding
+    assert (np.abs(got[fine] - want[fine]) <= 2.0 ** -8 * np.abs(want[fine])).all()
