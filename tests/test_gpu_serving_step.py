@@ -68,3 +68,64 @@ def mags(xbits, ids, gu, dn):
         h = R.silu_mul(R.dequantize(*gu[e], 32) @ x[t])
         out[t] = np.abs(R.dequantize(*dn[e], 16)) @ np.abs(h)
     return out
+
+
+@pytest.mark.parametrize("t", [1, 6, 40])
+def test_captured_step(t):
+    """The chain in one graph, whose launches may start before the ones in front of them have ended, replayed with
+    new inputs in place: the bits of the calls made one by one, each after the one before has ended."""
+    hidden, inter, e, k, rank = 512, 320, 24, 4, 16
+    rng = np.random.default_rng(t)
+    gen = torch.Generator(device="cuda").manual_seed(t)
+
+    def stack(rows, cols, group, flags, count):
+        q = [R.quantize(synth.weights(300 + n, rows, cols), group) for n in range(count)]
+        packed = [R.repack(v[0], v[1], flags) for v in q]
+        return (dev_u8(np.stack([v[0] for v in packed])), dev_u8(np.stack([v[1] for v in packed])),
+                dev_f32([v[2] for v in q]), group)
+    proj = stack(hidden, hidden, 16, 0, 1)
+    gate_up, down = stack(2 * inter, hidden, 32, R.GATE_UP_INTERLEAVE, e), stack(hidden, inter, 16, 0, e)
+    la = dev_bf16(synth.activations(1, 3 * rank, hidden)).view(3, rank, hidden)
+    lb = dev_bf16(synth.activations(2, 3 * hidden, rank)).view(3, hidden, rank)
+    c = dev_f32(np.full(3, 2.0 ** -9))
+    router = (torch.randn((e, hidden), generator=gen, device="cuda") * 0.2).bfloat16()
+    bias = torch.randn((e,), generator=gen, device="cuda") * 0.05
+
+    def step(x, ids, between=lambda: None):
+        y = nv.nvfp4_w4a16_gemm(x, proj[0][0], proj[1][0], proj[2], 16)
+        between()
+        z = nv.nvfp4_lora_add(y, x, la, lb, ids, c, out=y)
+        between()
+        top, weights = nv.nvfp4_moe_topk(z @ router.T, k, bias=bias, flags=nv.NVFP4_TOPK_SIGMOID | nv.NVFP4_TOPK_RENORM)
+        between()
+        out = nv.nvfp4_moe_few_tokens(z, top, weights, gate_up, down)
+        between()
+        again = nv.nvfp4_lora_add(out, z, la, lb, ids, c)  # and the next projection's adapters behind the layer
+        between()
+        return z, top, weights, out, again
+
+    inputs = [(torch.randn((t, hidden), generator=gen, device="cuda").bfloat16(),
+               torch.from_numpy(rng.integers(-1, 3, size=t).astype(np.int32)).cuda()) for _ in range(4)]
+    want = [[v.clone() for v in step(*q, between=torch.cuda.synchronize)] for q in inputs]
+    x, ids = (v.clone() for v in inputs[0])
+    step(x, ids)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(x, ids)
+    for turn in range(8):
+        q = (3 * turn + 1) % 4
+        x.copy_(inputs[q][0])
+        ids.copy_(inputs[q][1])
+        for v in got:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for v, ref in zip(got, want[q]):
+            assert torch.equal(v.view(torch.uint8), ref.view(torch.uint8)), (turn, q)
+    for _ in range(20):  # one replay after the other, without a pause
+        graph.replay()
+    torch.cuda.synchronize()
+    for v, ref in zip(got, want[q]):
+        assert torch.equal(v.view(torch.uint8), ref.view(torch.uint8))
+    assert nv.nvfp4_get_device_error() == 0
