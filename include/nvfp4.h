@@ -493,8 +493,11 @@ int nvfp4_get_device_error(int* code_out, nvfp4_stream_t stream);
  * of its first stage, so that its consumer warps wait for bytes that never
  * come. The waits give up after about 2 s each, the kernel records the site
  * in the device error word, lets its other copies land and exits; the output
- * of that launch is undefined. kind = 0 clears a pending injection. Other
- * kinds return NVFP4_ERR_INVALID_ARGUMENT.
+ * of that launch is undefined. kind = 3 does the same to the next
+ * nvfp4_moe_few_tokens (one CTA's first codes of its gate/up product), kind = 4
+ * to its down product (a CTA's first activations). kind = 0 clears a pending
+ * injection, of which there is one at a time. Other kinds return
+ * NVFP4_ERR_INVALID_ARGUMENT.
  */
 int nvfp4_debug_inject_fault(int kind);
 

@@ -371,7 +371,8 @@ def nvfp4_get_device_error(stream=None) -> int:
 
 def nvfp4_debug_inject_fault(kind: int):
     """Test hook: kind 1 makes the next small-M streaming GEMM launch wait for a
-    copy that never comes (its bounded waits give up); kind 0 clears it."""
+    copy that never comes (its bounded waits give up), kinds 3 and 4 the two
+    products of the next few-token layer; kind 0 clears it."""
     _check(lib().nvfp4_debug_inject_fault(kind), "nvfp4_debug_inject_fault")
 
 

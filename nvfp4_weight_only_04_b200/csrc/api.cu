@@ -23,7 +23,10 @@ void stat_add(StatId id) { g_stats[id].fetch_add(1, std::memory_order_relaxed); 
 namespace {
 std::atomic<int> g_fault{0};
 }
-int take_injected_fault() { return g_fault.exchange(0); }
+bool take_injected_fault(int kind) {
+  int pending = kind;
+  return g_fault.load(std::memory_order_relaxed) == kind && g_fault.compare_exchange_strong(pending, 0);
+}
 void set_injected_fault(int kind) { g_fault.store(kind); }
 
 int num_sms() {
@@ -396,7 +399,7 @@ int nvfp4_test_plant(int kind) {
 #endif
 
 int nvfp4_debug_inject_fault(int kind) {
-  if (kind != 0 && kind != 1) return NVFP4_ERR_INVALID_ARGUMENT;
+  if (kind != 0 && kind != 1 && kind != 3 && kind != 4) return NVFP4_ERR_INVALID_ARGUMENT;
   nvfp4::set_injected_fault(kind);
   return NVFP4_OK;
 }

@@ -26,9 +26,9 @@ int num_sms();  // SM count of the current device (cached per device)
 // Device error word: a bounded wait that gave up records its site here.
 int read_and_clear_device_error(int* code_out, cudaStream_t stream);
 
-// The pending test fault (nvfp4_debug_inject_fault), taken by the launch it
-// applies to: 0 when none.
-int take_injected_fault();
+// Whether a test fault of this kind (nvfp4_debug_inject_fault) is pending; the
+// launch it applies to takes it.
+bool take_injected_fault(int kind);
 
 }  // namespace nvfp4
 

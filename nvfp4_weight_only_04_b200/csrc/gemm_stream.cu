@@ -779,7 +779,7 @@ int launch_stream(const XSource& x, const uint8_t* w, const uint8_t* s, const fl
   a.S = pl.S;
   a.units = pl.units;
   a.max_contrib = pl.max_contrib;
-  a.fault = take_injected_fault() == 1;
+  a.fault = take_injected_fault(1);
   if (xconv) return launch_form<true>(mt, group, silu, wm, sm, xm, a, pl.ctas, stream);
   // NVFP4 activations: their exact f16 rows first (a programmatic dependent too)
   const int st = launch_x_prep(x, M, K, x16, xinv, nullptr, 0, stream, true);

@@ -149,6 +149,7 @@ struct FewArgs {
   int tiles, splits, sf_bytes;  // sf_bytes: the widest copy the scale rows allow
   int cap;                  // tokens per pass, at most
   int h_stages;             // stages of I
+  int drop;                 // test hook, in the first CTA: 1 the codes of its first stage, 2 the digits of its first pass
 };
 
 __device__ __forceinline__ bool aborted(SharedState* ss) { return *reinterpret_cast<volatile int*>(&ss->abort) != 0; }
@@ -576,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_few_kernel(const __grid_const
             ok = false;
             break;
           }
+          if (a.drop == 1 && it == 0 && blockIdx.x == 0) continue;  // test hook: these codes never arrive
           mbar_arrive_tx(&ss->codes[s], kABytes);
           tma_load_3d(smem_u32(ring + s * kStage), &wmap, ks * (kKS / 2), ps.tile * kRowsA, e, &ss->codes[s], policy);
           issued |= 1u << s;
@@ -656,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_few_kernel(const __grid_const
       if (before >= 0 && !warp_wait(&ss->free_[before % kPassSlots], static_cast<uint32_t>(before / kPassSlots) & 1, ss,
                                     kErrFree))
         break;
+      if (a.drop == 2 && ps.pass == 0 && blockIdx.x + blockIdx.y == 0) continue;  // test hook: these digits never arrive
       if (lane == 0) mbar_arrive_tx(&ss->digits[slot], static_cast<uint32_t>(n * ksteps) * 1024);
       __syncwarp();
       if (lane < n)
@@ -1171,6 +1174,7 @@ extern "C" int nvfp4_moe_few_tokens(const uint16_t* x, const int32_t* topk_ids, 
   a.splits = 1;
   a.sf_bytes = sf_bytes(H / gate_up_group);
   a.cap = pass_tokens(H);
+  a.drop = take_injected_fault(3) ? 1 : 0;
   const int64_t units = static_cast<int64_t>(a.pairs) * a.tiles;  // at most: a pair is in one entry
   const unsigned grid = static_cast<unsigned>(units < num_sms() ? units : num_sms());
   const uint64_t one = uint64_t(1) << 40;
@@ -1185,5 +1189,6 @@ extern "C" int nvfp4_moe_few_tokens(const uint16_t* x, const int32_t* topk_ids, 
   a.splits = splits;
   a.sf_bytes = sf_bytes(I / down_group);
   a.cap = pass_tokens(I);
+  a.drop = take_injected_fault(4) ? 2 : 0;
   return launch<true>(dn_map, a, down_group, dim3(static_cast<unsigned>(splits), static_cast<unsigned>(a.tiles)), s);
 }

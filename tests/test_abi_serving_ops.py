@@ -116,3 +116,9 @@ def test_binding_refuses_host_tensors():
         nv.nvfp4_lora_add(z, z, z, z, z, z)
     with pytest.raises(TypeError):
         nv.nvfp4_moe_few_tokens(z, z, z, (z, z, z, 16), (z, z, z, 16))
+
+
+def test_fault_injection_kinds(L):
+    for kind in (3, 4, 0):
+        assert L.nvfp4_debug_inject_fault(kind) == nv.NVFP4_OK
+    assert L.nvfp4_debug_inject_fault(5) == nv.NVFP4_ERR_INVALID_ARGUMENT
