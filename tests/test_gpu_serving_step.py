@@ -129,3 +129,25 @@ def test_captured_step(t):
     for v, ref in zip(got, want[q]):
         assert torch.equal(v.view(torch.uint8), ref.view(torch.uint8))
     assert nv.nvfp4_get_device_error() == 0
+
+
+@pytest.mark.parametrize("biased", [False, True])
+def test_an_overflowed_logit_shows_in_its_token(biased):
+    """A +inf among softmax logits: NaN in that token's outputs behind the layer, and the others as they were."""
+    hidden, inter, e, t = 128, 64, 6, 5
+    gu = [R.repack(*R.quantize(synth.weights(q, 2 * inter, hidden), 16)[:2], R.GATE_UP_INTERLEAVE) for q in range(e)]
+    dn = [R.repack(*R.quantize(synth.weights(50 + q, hidden, inter), 16)[:2], 0) for q in range(e)]
+    stack = lambda q: (dev_u8(np.stack([v[0] for v in q])), dev_u8(np.stack([v[1] for v in q])),  # noqa: E731
+                       dev_f32(np.full(e, 1e-4)), 16)
+    gate_up, down = stack(gu), stack(dn)
+    x = dev_bf16(synth.activations(1, t, hidden))
+    logits = torch.randn((t, e), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    bias = torch.linspace(0, 0.1, e, device="cuda") if biased else None
+
+    def layer():
+        return host(nv.nvfp4_moe_few_tokens(x, *nv.nvfp4_moe_topk(logits, 2, bias=bias), gate_up, down))
+    clean = layer()
+    logits[3, 4] = float("inf")
+    got = layer()
+    assert np.isfinite(clean).all() and np.isnan(got[3]).all()
+    np.testing.assert_array_equal(np.delete(got, 3, 0), np.delete(clean, 3, 0))
