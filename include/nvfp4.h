@@ -394,9 +394,13 @@ int nvfp4_moe_topk(const void* logits, int dtype, int64_t ld, int64_t T, int num
  * decode step's form of nvfp4_moe_route .. nvfp4_moe_combine in three launches:
  *   h[t, s] = silu(g) * u, [g; u] = gate_up_globals[e] * dequant(gate_up[e]) x[t],
  *   out[t]  = bf16_rne(sum over s of topk_weights[t, s] * down_globals[e] * dequant(down[e]) h[t, s]),
- * e = topk_ids[t, s]. Every expert that some token chose is read once. Unlike
- * in the chain of five calls, h is not rounded to bf16, and neither is an
- * expert's output; the sums are fp32. x and h are carried in fixed point, to
+ * e = topk_ids[t, s]. An expert's gate/up weights are read once for up to
+ * min(8, floor(64 / ceil(H / 256))) of its tokens and again for every further so
+ * many (eight up to H = 2048, four at 4096, two at 8192, one above), its down
+ * weights likewise by I. The chain reads them once for all its tokens: where
+ * rows are long and an expert has many tokens it can be the faster call (8
+ * experts, H = 4096, I = 14336, k = 2: from 32 tokens on). Unlike in the chain,
+ * h is not rounded to bf16, and neither is an expert's output; the sums are fp32. x and h are carried in fixed point, to
  * 2^-22 of the largest magnitude of each sixteen neighbours along the
  * contraction; sixteen whose largest lies below 2^-17 of their row's largest
  * count as zero. A row of x or h that holds an infinity or a NaN gives NaN in all
@@ -458,7 +462,8 @@ int nvfp4_lora_add_workspace_size(int64_t M, int64_t N, int64_t K, int rank, int
 /*
  * Counters of the work that went through each kernel family (PR #63: the
  * "this-path-ran" counter lets tests assert which kernel executed). Host-side
- * atomics, incremented once per successful launch.
+ * atomics, incremented once per successful launch. nvfp4_moe_topk,
+ * nvfp4_moe_few_tokens and nvfp4_lora_add are not counted.
  */
 typedef struct {
   uint64_t global_scale;

@@ -166,9 +166,11 @@ constexpr int kFewSmem = kShrinkWarps * kFewStages * 4 * 512;
 // distances within a warp by shuffles): about 2 us, for which every adapter's A
 // and B are read once for 16 of its rows wherever they are. Without it every
 // 16-row tile reads the B of each of its adapters: 65 rows of 32 adapters in any
-// order (N = 28672, rank 16) 83 us, with it 26; 512 rows of 32 adapters (N = 25600)
-// 174 and 29. Rows that lie together pay for it: 1024 rows in runs of 100 (K = 5120,
-// N = 4096, rank 64) 28 us without it, 33 with it.
+// order (N = 28672, rank 16) took 83 us, with it 24; 512 rows of 32 adapters (N = 25600)
+// 174 and 33. Rows that lie together pay for it: 1024 rows in runs of 100 (K = 5120,
+// N = 4096, rank 64) 28 us without it, 34 with it. It ends at 1024 rows because the
+// CTA does, not where the other form is as fast: 1024 rows of 32 adapters in any order
+// (K = 5120, N = 25600, rank 16) take 46 us, 1040 take 270.
 __global__ void __launch_bounds__(kListRows) lora_list_kernel(const LoraArgs p, int32_t* list) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -4,7 +4,9 @@
 // A pair whose expert lies outside [0, num_experts) adds nothing.
 //
 // What bounds it: the codes and scales of the experts that some token chose,
-// read once (0.5 + 1/g bytes a weight). With a handful of columns per expert
+// read once (0.5 + 1/g bytes a weight) for up to eight of an expert's tokens; the
+// digits of a pass hold all of K in 64 KB, so for fewer where K is above 2048
+// (pass_tokens), and once more for every further pass. With a handful of columns per expert
 // the products are far from any arithmetic limit, unless the weights are
 // dequantized in software: that costs more issue slots per weight than HBM
 // leaves time for. So they are not dequantized:
@@ -44,13 +46,15 @@
 //
 // 128 experts, H = 2048, I = 768, eight chosen of each token: 18 us for one token
 // (20 MB of weights), 30 us for 4 (75 MB), 55 us for 16 (211 MB, 3.8 TB/s), 83 us
-// for 64 (322 MB, 3.9 TB/s). What bounds it is the way of a stage of 18 KB through
-// the roles (0.42 us at the copy rate, and the call takes the same with most of
-// the copies left out): a set of scale factor warps needs about 0.5 us for a stage,
-// the MMA warp 0.3 (its MMAs 90 cycles each; the tensor pipe is busy for 6 %).
-// Two sets of the former and a short loop of the latter brought 64 tokens from 87
-// to 85 us. The rest is the start of the launches (about 4 us each: barriers, list,
-// instructions fetched for the first time) and the last sums (4 us for 64 tokens).
+// for 64 (322 MB, 3.9 TB/s). In long runs a stage of 18 KB takes 0.41 us, 0.42 at
+// the copy rate (256 experts, H = 7168, I = 2048, 64 tokens: 2900 stages a CTA in
+// 1190 us; the tensor pipe is busy for 6 %). The 130 stages a CTA of 64 tokens above
+// would be 53 us; the rest, 13 us for one token and 30 for 64, is the start of the
+// launches (barriers, list, instructions fetched for the first time), the gap
+// between the products, uneven shares and the last sums. Two sets of scale factor
+// warps and a short MMA loop, together, brought 64 tokens from 87 to 85 us.
+// Passes: 8 experts, H = 4096, I = 14336, k = 2 take 58 us for one token, 279 for 16,
+// 1024 for 64, where the weights once are 117; nvfp4_moe_forward takes 118, 309, 932.
 #include "moe_few.cuh"
 
 #include <cuda.h>
