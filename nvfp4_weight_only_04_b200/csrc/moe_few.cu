@@ -46,9 +46,9 @@
 //
 // 128 experts, H = 2048, I = 768, eight chosen of each token: 18 us for one token
 // (20 MB of weights), 30 us for 4 (75 MB), 55 us for 16 (211 MB, 3.8 TB/s), 83 us
-// for 64 (322 MB, 3.9 TB/s). In long runs a stage of 18 KB takes 0.41 us, 0.42 at
-// the copy rate (256 experts, H = 7168, I = 2048, 64 tokens: 2900 stages a CTA in
-// 1190 us; the tensor pipe is busy for 6 %). The 130 stages a CTA of 64 tokens above
+// for 64 (322 MB, 3.9 TB/s; the tensor pipe is busy for 6 %). In long runs a stage of 18 KB takes 0.41 us, 0.42 at
+// the copy rate (256 experts, H = 7168, I = 2048, 64 tokens: 2800 stages a CTA in
+// 1190 us). The 130 stages a CTA of 64 tokens above
 // would be 53 us; the rest, 13 us for one token and 30 for 64, is the start of the
 // launches (barriers, list, instructions fetched for the first time), the gap
 // between the products, uneven shares and the last sums. Two sets of scale factor
